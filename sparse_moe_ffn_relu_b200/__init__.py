@@ -426,13 +426,27 @@ def _matrix(t: torch.Tensor, what: str):
     return t.shape
 
 
-def _gate_kind(gate, T: int, D: int) -> int:
-    """0 none, 1 per channel [D] fp32, 2 per token [T] or [T][1] fp32, 3 full [T][D].
-    A gate [n] with n = T = D is per channel; give [T][1] for the other."""
+_GATES = {"channel": 1, "token": 2, "full": 3}     # deco_gate_t
+
+
+def _gate_kind(gate, T: int, D: int, kind=None) -> int:
+    """deco_gate_t of a gate, by its shape: [D] per channel, [T] or [T][1] per
+    token, [T][D] full.  kind ("channel", "token", "full") names it, which a
+    gate [n] with n = T = D needs."""
     if gate is None:
+        if kind is not None:
+            raise ValueError(f"gate_kind {kind!r} without a gate")
         return 0
     shape = gate.shape
+    if kind is not None:
+        if kind not in _GATES:
+            raise ValueError(f"gate_kind: expected one of {tuple(_GATES)}, got {kind!r}")
+        if shape != {"channel": (D,), "token": (T,), "full": (T, D)}[kind] and not (kind == "token" and shape == (T, 1)):
+            raise ValueError(f"gate: {tuple(shape)} is not a {kind} gate of {T} tokens of {D} channels")
+        return _GATES[kind]
     if shape == (D,):
+        if T == D and D > 1:
+            raise ValueError(f"gate: [{D}] with {T} tokens of {D} channels is per channel or per token: name it with gate_kind")
         return 1
     if shape == (T, D) and not (D == 1 and gate.dtype is _F32):
         return 3
@@ -442,24 +456,25 @@ def _gate_kind(gate, T: int, D: int) -> int:
 
 
 def block_norm(x: torch.Tensor, g_pre=None, y=None, g_post=None, gate=None, branch_scale: float = 1.0,
-               eps=1e-6, out=None, h=None, stream=None):
+               eps=1e-6, out=None, h=None, stream=None, gate_kind=None):
     """(out, h) with out = x + branch_scale * gate * RMSNorm(y) * g_post and
     h = RMSNorm(out) * g_pre: the norm, gate and residual scale behind a block
     and the norm before the next, in one pass.
 
     x, y [T][D] fp32 or bf16; g_pre, g_post [D] fp32.  gate: [D] fp32 (per
-    channel), [T] or [T][1] fp32 (per token) or [T][D] (x's type).  Without y,
-    h = RMSNorm(x) * g_pre and out is None.  Without g_post y is added as it
+    channel), [T] or [T][1] fp32 (per token) or [T][D] (x's type); gate_kind
+    "channel", "token" or "full" says which, and has to where a gate has one
+    dimension and T = D > 1.  Without y, h = RMSNorm(x) * g_pre and out is None.  Without g_post y is added as it
     is; without g_pre there is no h.  out may be x."""
     ctx = _elsewhere(x, stream)
     if ctx is not None:
         with ctx:
-            return block_norm(x, g_pre, y, g_post, gate, branch_scale, eps, out, h)
+            return block_norm(x, g_pre, y, g_post, gate, branch_scale, eps, out, h, None, gate_kind)
     dt, dtype, dev, shape = _storage(x, "x"), x.dtype, x.get_device(), _matrix(x, "x")
     T, D = shape
     px, ld_x = _rows(x, "x", shape, dtype, dev)
     py, ld_y = _rows(y, "y", shape, dtype, dev)
-    kind, ld_gate = _gate_kind(gate, T, D), 0
+    kind, ld_gate = _gate_kind(gate, T, D, gate_kind), 0
     if kind == 3:
         p_gate, ld_gate = _rows(gate, "gate", shape, dtype, dev)
     else:
@@ -487,7 +502,7 @@ def _norm_workspace(T: int, D: int, dt: int, dev: int) -> int:
 
 
 def block_norm_backward(x: torch.Tensor, g_pre=None, y=None, g_post=None, gate=None, branch_scale: float = 1.0,
-                        eps=1e-6, dout=None, dh=None, dx=None, workspace=None, stream=None) -> dict:
+                        eps=1e-6, dout=None, dh=None, dx=None, workspace=None, stream=None, gate_kind=None) -> dict:
     """Gradients of block_norm: a dict of dx, dy, dg_pre, dg_post, dgate (those
     that exist).  x is the sum the forward pass stored (its out, or its x where
     it had no y).  dout: gradient with respect to out apart from h's share, dh:
@@ -495,18 +510,18 @@ def block_norm_backward(x: torch.Tensor, g_pre=None, y=None, g_post=None, gate=N
     (the type of backward()'s dx); dx comes in dout's type (x's without dout)
     and may be dout.  dg_pre, dg_post and the gradients of [D] and [T] gates
     are fp32, dy and a [T][D] gate's gradient in x's type.  Without dh, g_pre
-    is not used."""
+    is not used.  gate_kind as in block_norm."""
     ctx = _elsewhere(x, stream)
     if ctx is not None:
         with ctx:
-            return block_norm_backward(x, g_pre, y, g_post, gate, branch_scale, eps, dout, dh, dx, workspace)
+            return block_norm_backward(x, g_pre, y, g_post, gate, branch_scale, eps, dout, dh, dx, workspace, None, gate_kind)
     dt, dtype, dev, shape = _storage(x, "x"), x.dtype, x.get_device(), _matrix(x, "x")
     T, D = shape
     if dh is None:
         g_pre = None
     px, ld_x = _rows(x, "x", shape, dtype, dev)
     py, ld_y = _rows(y, "y", shape, dtype, dev)
-    kind, ld_gate = _gate_kind(gate, T, D), 0
+    kind, ld_gate = _gate_kind(gate, T, D, gate_kind), 0
     if kind == 3:
         p_gate, ld_gate = _rows(gate, "gate", shape, dtype, dev)
     else:

@@ -174,3 +174,23 @@ def test_the_binding_checks_its_tensors(deco):
     assert [deco._gate_kind(g, 4, 64) for g in (None, torch.zeros(64), torch.zeros(4), torch.zeros(4, 1), torch.zeros(4, 64))] == [0, 1, 2, 2, 3]
     with pytest.raises(ValueError, match="gate"):
         deco._gate_kind(torch.zeros(5), 4, 64)
+
+
+def test_a_gate_of_as_many_tokens_as_channels_is_named(deco):
+    """[n] with n = T = D could be a gate per channel or per token: the binding
+    asks for its kind instead of taking one of them."""
+    n, kind = torch.zeros(8), deco._gate_kind
+    with pytest.raises(ValueError, match="gate_kind"):
+        kind(n, 8, 8)
+    assert [kind(n, 8, 8, k) for k in ("channel", "token")] == [1, 2]
+    assert kind(torch.zeros(8, 1), 8, 8) == kind(torch.zeros(8, 1), 8, 8, "token") == 2       # shapes that say it
+    assert kind(torch.zeros(8, 8), 8, 8) == kind(torch.zeros(8, 8), 8, 8, "full") == 3
+    assert kind(torch.zeros(1), 1, 1) == 1                                                    # one value: the same either way
+    assert [kind(torch.zeros(s), 4, 8, k) for s, k in (((8,), "channel"), ((4,), "token"), ((4, 1), "token"), ((4, 8), "full"))] == [1, 2, 2, 3]
+    assert [kind(torch.zeros(4, 1), 4, 1, k) for k in ("token", "full")] == [2, 3]            # of one channel
+    for shape, k in (((8,), "token"), ((4,), "channel"), ((4, 8), "token"), ((8,), "full"), ((4, 1), "full"), ((8,), "rows")):
+        with pytest.raises(ValueError, match="gate"):
+            kind(torch.zeros(shape), 4, 8, k)
+    with pytest.raises(ValueError, match="gate"):
+        kind(None, 4, 8, "token")
+    assert kind(None, 4, 8) == 0
