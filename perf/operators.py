@@ -298,16 +298,22 @@ def _plain_q4_experts(s):
 
 # ---- this framework's kernels -------------------------------------------------
 
+def _gate_kind(c):
+    """The gate's kind, where a batch of as many tokens as channels leaves it open."""
+    return {"gate_kind": c["gate"]} if c["T"] == c["D"] and c["gate"] in ("channel", "token") else {}
+
+
 def _own(s):
     import sparse_moe_ffn_relu_b200 as deco
 
     kind = s["case"]["kind"]
     if kind == "norm":
-        out, h = deco.block_norm(s["x"], s["g_pre"], y=s["y"], g_post=s["g_post"], gate=s["gate"], branch_scale=s["branch_scale"], eps=EPS)
+        out, h = deco.block_norm(s["x"], s["g_pre"], y=s["y"], g_post=s["g_post"], gate=s["gate"], branch_scale=s["branch_scale"], eps=EPS,
+                                **_gate_kind(s["case"]))
         return {"out": out, "h": h}
     if kind == "norm_bwd":
         return deco.block_norm_backward(s["x"], s["g_pre"], y=s["y"], g_post=s["g_post"], gate=s["gate"], branch_scale=s["branch_scale"], eps=EPS,
-                                        dout=s["dout"], dh=s["dh"])
+                                        dout=s["dout"], dh=s["dh"], **_gate_kind(s["case"]))
     if kind == "dispatch":
         return deco.dispatch(s["x"], E=s["case"]["E"], out=s["out"], **s["how"])
     if kind == "combine":
