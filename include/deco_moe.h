@@ -522,7 +522,9 @@ deco_status_t deco_q4_matvec(int T, int N, int K, int group, int dtype, int out_
  * (ascending, as deco_moe_routing and deco_moe_dispatch write them) are
  * multiplied by W[e]: y[i] = W[e] x[perm ? perm[i] : i].  perm (row of x of
  * each sorted row: the perm of deco_moe_routing) spares the sorted copy of x;
- * a number outside 0..rows_x-1 gives a zero row.  rows_x <= 2^28; rows_y: rows
+ * a number outside 0..rows_x-1 gives a zero row, so with rows_x = 0 (x is not
+ * read then and may be NULL) all of them are zeros.  rows_x = 0 without perm
+ * does nothing.  rows_x <= 2^28; rows_y: rows
  * that y (and perm) hold, <= 2^28; rows at or beyond it are not touched, nor are rows of y
  * behind offsets[E].  Only experts that have rows are read.  E <= 256. */
 deco_status_t deco_q4_expert_matvec(int E, int N, int K, int group, int dtype, int out_dtype, const int* offsets,

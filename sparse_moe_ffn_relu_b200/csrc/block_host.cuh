@@ -320,8 +320,9 @@ deco_status_t q4_product(int N, int K, int group, int dtype, int out_dtype, int 
   const long long units = (long long)(N / 16 + 1) * (std::min<long long>(E, rows_y) + rows_y / 8 + 1);
   if (units > 0x7fffffffll || units * (q4_padded(K) / q4::kBlock) > (1ll << 36)) return DECO_ERR_UNSUPPORTED;   // also a CTA's steps
   if (!resolve_ld(ld_x, K) || !resolve_ld(ld_y, N)) return DECO_ERR_INVALID_ARG;
-  if (rows_x == 0 || rows_y == 0) return DECO_OK;
-  if (!x || !q || !scale || !y || x == y) return DECO_ERR_INVALID_ARG;
+  // perm into an x of no rows asks for zero rows
+  if (rows_y == 0 || (rows_x == 0 && !perm)) return DECO_OK;
+  if ((!x && rows_x) || !q || !scale || !y || x == y) return DECO_ERR_INVALID_ARG;
   if (!aligned_to(x, elem_size(dtype)) || !aligned_to(y, elem_size(out_dtype)) || !aligned16(q) || !aligned_to(scale, 8) ||
       (zero && !aligned_to(zero, 4)))
     return DECO_ERR_INVALID_ARG;
@@ -335,7 +336,7 @@ deco_status_t q4_product(int N, int K, int group, int dtype, int out_dtype, int 
   a.q = static_cast<const unsigned char*>(q);
   a.scale = static_cast<const unsigned char*>(scale);
   a.zero = zero;
-  a.x = x;
+  a.x = rows_x ? x : q;   // an address even where there is nothing to read: copies of zeros name one
   a.y = y;
   a.ld_x = ld_x;
   a.ld_y = ld_y;

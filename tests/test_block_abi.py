@@ -194,3 +194,14 @@ def test_a_gate_of_as_many_tokens_as_channels_is_named(deco):
     with pytest.raises(ValueError, match="gate"):
         kind(None, 4, 8, "token")
     assert kind(None, 4, 8) == 0
+
+
+def test_q4_experts_without_rows_of_x_still_check_perm(deco):
+    """perm into an x of no rows asks for zero rows, so its call is one like
+    others; without perm there is nothing to do.  (Refusals alone: nothing
+    here reaches a device.)"""
+    def ex(rx=0, x=None, off=GQ, perm=H, y=OUT, ry=16, q=Y):
+        return deco._lib.deco_q4_expert_matvec(8, 32, 128, 64, 1, 1, off, perm, rx, x, 0, q, GP, None, ry, y, 0, None)
+    for kw in (dict(perm=H + 2), dict(off=None), dict(y=None), dict(q=None), dict(rx=4), dict(y=OUT + 1)):
+        assert ex(**kw) == INVALID, kw
+    assert ex(perm=None) == OK and ex(ry=0) == OK
