@@ -362,9 +362,14 @@ def sparsity_controller(lam: float, ratio: float, target: float, factor: float =
 # device's current stream; what they allocate belongs to that stream.
 
 # Small calls are bound by the time this module takes, so the checks below look
-# at each property once, with PyTorch's cheapest accessors.
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream     # of a device, as an integer
+# at each property once, with PyTorch's cheapest accessors; builds of PyTorch
+# that lack the private ones have the public calls.
+def _public_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)     # of a device, as an integer
 _F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 
 

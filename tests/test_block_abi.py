@@ -2,6 +2,9 @@
 the host before anything is launched.  No GPU is needed: the pointers are made
 up and no call reaches the device."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -205,3 +208,25 @@ def test_q4_experts_without_rows_of_x_still_check_perm(deco):
     for kw in (dict(perm=H + 2), dict(off=None), dict(y=None), dict(q=None), dict(rx=4), dict(y=OUT + 1)):
         assert ex(**kw) == INVALID, kw
     assert ex(perm=None) == OK and ex(ry=0) == OK
+
+
+def test_import_needs_no_private_name_of_pytorch():
+    """Where a build of PyTorch lacks the quick accessors of device and stream,
+    the public ones serve."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import sparse_moe_ffn_relu_b200 as deco
+assert deco._current_device is torch.cuda.current_device
+class Stream:
+    cuda_stream = 1234
+torch.cuda.current_stream = lambda device: Stream() if device == 3 else None
+assert deco._raw_stream(3) == 1234
+assert deco.sparsity_controller(1.0, 0.3, 0.2) > 1.0      # calls that need no GPU
+print("imported")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "imported", r.stdout + r.stderr
