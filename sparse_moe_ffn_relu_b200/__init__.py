@@ -425,10 +425,21 @@ def _storage(t: torch.Tensor, what: str) -> int:
     return dt
 
 
-def _matrix(t: torch.Tensor, what: str):
-    if t.dim() != 2:
-        raise ValueError(f"{what}: expected two dimensions, got {tuple(t.shape)}")
-    return t.shape
+# The C side takes most sizes as 32-bit integers, and ctypes cuts what it is
+# given to that without a word.
+def _matrix(t: torch.Tensor, what: str, row_bits: int = 31):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what}: expected two dimensions, got {tuple(shape)}")
+    if shape[0] >> row_bits or shape[1] >> 31:
+        raise ValueError(f"{what}: {tuple(shape)} has a size of 2^31 or more")
+    return shape
+
+
+def _experts(E: int) -> int:
+    if E >> 31:
+        raise ValueError(f"E: expected a number below 2^31, got {E}")
+    return E
 
 
 _GATES = {"channel": 1, "token": 2, "full": 3}     # deco_gate_t
@@ -607,6 +618,7 @@ def dispatch(x, E=None, experts=None, active=None, capacity=None, out=None, work
     else:
         if E is None:
             raise ValueError("dispatch: E is needed with experts")
+        E = _experts(E)
         p_experts = _whole(experts, "experts", shape, _I32, dev)
     D, dt, px, ld_x = 1, DECO_F32, None, 0
     if x is not None:
@@ -655,7 +667,7 @@ def combine(ys: torch.Tensor, row_of: torch.Tensor, w=None, base=None, out=None,
             return combine(ys, row_of, w, base, out, out_dtype)
     dt, dtype, dev, table = _storage(ys, "ys"), ys.dtype, ys.get_device(), _matrix(row_of, "row_of")
     T, S = table
-    n, D = _matrix(ys, "ys")
+    n, D = _matrix(ys, "ys", 63)
     p_ys, ld_ys = _rows(ys, "ys", (n, D), dtype, dev)
     p_base, ld_base = _rows(base, "base", (T, D), dtype, dev)
     if out is None:
@@ -681,7 +693,7 @@ def combine_backward(ys: torch.Tensor, row_of: torch.Tensor, w, dy: torch.Tensor
             return combine_backward(ys, row_of, w, dy, dys)
     dt, dtype, dev, table = _storage(ys, "ys"), ys.dtype, ys.get_device(), _matrix(row_of, "row_of")
     T, S = table
-    n, D = _matrix(ys, "ys")
+    n, D = _matrix(ys, "ys", 63)
     p_ys, ld_ys = _rows(ys, "ys", (n, D), dtype, dev)
     p_dy, ld_dy = _rows(dy, "dy", (T, D), dtype, dev)
     if dys is None:
@@ -708,6 +720,8 @@ def _q4_sizes(K: int, group: int):
     """Bytes of codes and number of groups of a row, its padding included."""
     if group not in Q4_GROUPS:
         raise ValueError(f"group: expected one of {Q4_GROUPS}, got {group}")
+    if K >> 31:
+        raise ValueError(f"K: expected a number below 2^31, got {K}")
     Kp = -(-K // 128) * 128
     return Kp // 2, Kp // group
 

@@ -230,3 +230,26 @@ print("imported")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "imported", r.stdout + r.stderr
+
+
+def test_sizes_beyond_32_bits_are_refused(deco):
+    """The C side takes sizes as 32-bit integers, which ctypes fills with the
+    low bits of what it gets: 2^32 + 4 rows must not become four."""
+    far = 2 ** 32 + 4
+    for shape in ((far, 1), (2 ** 31, 1), (1, far), (3, 2 ** 31)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            deco._matrix(torch.empty(shape, device="meta"), "x")
+    assert deco._matrix(torch.empty(2 ** 31 - 1, 1, device="meta"), "x") == (2 ** 31 - 1, 1)
+    # rows that only a table of int32 names may be more: their number is 64 bits wide in C
+    assert deco._matrix(torch.empty(far, 1, device="meta"), "ys", 63) == (far, 1)
+    with pytest.raises(ValueError, match="2\\^31"):
+        deco._matrix(torch.empty(1, far, device="meta"), "ys", 63)
+    for K in (2 ** 32 + 128, 2 ** 31):
+        with pytest.raises(ValueError, match="2\\^31"):
+            deco._q4_sizes(K, 64)
+    with pytest.raises(ValueError, match="dimensions"):
+        deco._matrix(torch.zeros(4), "x")
+    # every size that a call takes goes through one of these, but for dispatch's E
+    with pytest.raises(ValueError, match="2\\^31"):
+        deco._experts(2 ** 32 + 3)
+    assert deco._experts(256) == 256
