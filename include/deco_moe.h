@@ -395,9 +395,11 @@ typedef struct {
  * g_post, g_pre: fp32 [D].  y and out are both given or both NULL (NULL: no
  * block in front, h = n(x) * g_pre; then no g_post and no gate).  g_post NULL:
  * no norm behind the block, y itself is added.  g_pre and h are both given or
- * both NULL.  out may be x (the same stride).  Mean squares are fp32: they
- * overflow for rows of values beyond about 1e18, and a zero row with eps = 0
- * gives NaN (0 / 0). */
+ * both NULL.  out may be x (the same stride).  A mean square is an fp32 sum of
+ * squares times 1 / D: the sum has to stay below 3.4e38, so a row's root mean
+ * square below 1.8e19 / sqrt(D) (2.8e17 at D = 4096; beyond it the normalised
+ * row is 0).  With eps = 0 it has to be 1e-18 or more (the squares of smaller
+ * values lose bits, and a row whose squares are all 0 gives NaN, 0 / 0). */
 deco_status_t deco_block_norm_forward(const deco_block_norm_t* shape, const void* x, const void* y,
                                       const float* g_post, const void* gate, const float* g_pre,
                                       void* out, void* h, void* stream);
@@ -421,7 +423,9 @@ deco_status_t deco_block_norm_backward_workspace_size(const deco_block_norm_t* s
  * read only with dh.  dout: gradient of the loss with respect to out without
  * the share that goes through h; dh: with respect to h; either may be NULL,
  * not both, and g_pre is given iff dh is.  dx is the gradient with respect to
- * the forward pass's x.  dx may be dout.  T = 0 writes zeros to dg_pre,
+ * the forward pass's x.  dx may be dout.  Its sums over a row, of the squares
+ * of x and y and of the products of two of dout, dh g_pre, x and y gate g_post,
+ * are fp32 and have to stay in its range.  T = 0 writes zeros to dg_pre,
  * dg_post and a channel gate's gradient.  The workspace (256-byte aligned) is
  * the caller's; its contents need no initialisation. */
 deco_status_t deco_block_norm_backward(const deco_block_norm_t* shape, const void* x, const void* y,
@@ -496,7 +500,7 @@ deco_status_t deco_moe_combine_backward(int T, int slots, int d_model, int dtype
  * Padding (codes, scales and zeros of columns K..Kp-1) is never used.  A set of
  * E experts' matrices is one of E * N rows.  rows <= 2^28, K <= 2^20. */
 
-/* Quantises W (dtype, [rows][K] without gaps, finite): symmetric (zero NULL)
+/* Quantises W (dtype, [rows][K] without gaps, magnitudes up to 1e38): symmetric (zero NULL)
  * with scale = max|w| / 7 and code = round(w / scale) + 8, or with
  * lo = min(w, 0), hi = max(w, 0), scale = (hi - lo) / 15,
  * zero = round(-lo / scale) and code = round(w / scale) + zero; the scale
@@ -511,7 +515,9 @@ deco_status_t deco_q4_dequantize(long long rows, int K, int group, int dtype, co
                                  const uint8_t* zero, void* W, void* stream);
 
 /* y[T][N] = x[T][K] W^T with the 4-bit W [N][K].  x in `dtype`; y in out_dtype:
- * dtype or fp32 (fp32 x: fp32 y).  Products are exact, sums fp32.  Made for
+ * dtype or fp32 (fp32 x: fp32 y).  Products are exact, sums fp32; a group's sum
+ * of x (code - zero) is formed before its scale comes to it and has to be in
+ * fp32's range (for x up to 1.7e35 it always is).  Made for
  * the few rows of a decode batch, though any T up to 2^28 works (units of 16
  * rows of W and 8 of x are counted in 32 bits; more is refused). */
 deco_status_t deco_q4_matvec(int T, int N, int K, int group, int dtype, int out_dtype, const void* x, long long ld_x,
