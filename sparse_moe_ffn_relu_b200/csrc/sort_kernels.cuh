@@ -211,7 +211,8 @@ __device__ __forceinline__ void copy_rows(const Args& a, const uint16_t* slot, i
 // STEPS: 32-slot steps of a warp at most
 template <typename V, int STEPS>
 __global__ void __launch_bounds__(kSmallThreads) ks_small(const Args a) {
-  __shared__ uint16_t whist[kSmallWarps][kMaxE];   // counts and rows up to 16384
+  __shared__ __align__(4) uint16_t whist[kSmallWarps][kMaxE];   // counts and rows up to 16384
+  static_assert(__alignof__(whist) >= alignof(uint32_t), "zeroed by words");
   extern __shared__ uint16_t s_slot[];             // [slots]
   __shared__ int wsum[kSmallWarps];
   const int n = a.T * a.S, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
