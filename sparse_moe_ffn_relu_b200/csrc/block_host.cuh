@@ -217,6 +217,9 @@ bool q4_blocks_ok(long long rows, int K, unsigned* ctas) {
   return n <= 0x7fffffffll;
 }
 
+// at most 2^this warps share a row's K
+template <typename T> constexpr int kQ4MostSplit = sizeof(T) == 4 ? 3 : 4;
+
 struct Q4Plan {
   int m, split, cluster;      // row tiles a warp; warps a row, CTAs a row (log2)
   long long units;
@@ -225,7 +228,7 @@ struct Q4Plan {
 template <typename T, int NT, int M, int G>
 cudaError_t q4_launch(q4::Args& a, const Q4Plan& p, cudaStream_t st) {
   using S = q4::Smem<T, NT, M>;
-  static_assert(S::kMaxBlocks >= 8, "q4_plan's largest split has room for its blocks");
+  static_assert(S::kMaxBlocks >= 1 << kQ4MostSplit<T>, "the largest split has room for a block of x a warp");
   const int blocks = (a.Kp / q4::kBlock + (1 << p.cluster) - 1) >> p.cluster, bpw = (blocks + (1 << p.split) - 1) >> p.split;
   a.split_log2 = p.split;
   a.cluster_log2 = p.cluster;
@@ -258,7 +261,6 @@ cudaError_t q4_launch(q4::Args& a, const Q4Plan& p, cudaStream_t st) {
 template <typename T>
 Q4Plan q4_plan(int N, int blocks, int nt, long long items, long long likely, int sms) {
   constexpr bool kF32 = sizeof(T) == 4;
-  const int most_split = kF32 ? 3 : 4;
   const auto room = [&](int m) {   // blocks of x that fit
     if (kF32) return nt == 1 ? q4::Smem<T, 1, 1>::kMaxBlocks : q4::Smem<T, 2, 1>::kMaxBlocks;
     if (nt == 4) return q4::Smem<T, 4, 1>::kMaxBlocks;
@@ -268,7 +270,7 @@ Q4Plan q4_plan(int N, int blocks, int nt, long long items, long long likely, int
   Q4Plan best{1, 0, 0, 0};
   double least = 1e30;
   for (int m = 1; m <= (nt == 4 || kF32 ? 1 : 2); ++m)
-    for (int s = 0; s <= most_split && (s == 0 || (1 << s) <= blocks); ++s) {
+    for (int s = 0; s <= kQ4MostSplit<T> && (s == 0 || (1 << s) <= blocks); ++s) {
       const int width = (q4::kWarps >> s) * 16 * m;
       const long long tiles = (N + width - 1) / width;
       for (int c = 0; (1 << c) <= (width <= q4::kClusterWidth ? q4::kMaxCluster : 1) && (c == 0 || (1 << (s + c)) <= blocks); ++c) {
