@@ -431,7 +431,7 @@ def _matrix(t: torch.Tensor, what: str, row_bits: int = 31):
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{what}: expected two dimensions, got {tuple(shape)}")
-    if shape[0] >> row_bits or shape[1] >> 31:
+    if t.numel() >> 31 and (shape[0] >> row_bits or shape[1] >> 31):
         raise ValueError(f"{what}: {tuple(shape)} has a size of 2^31 or more")
     return shape
 
