@@ -288,7 +288,10 @@ Q4Plan q4_plan(int N, int blocks, int nt, long long items, long long likely, int
 }
 
 // The launch of a product: `most` is the largest number of rows one matrix can
-// meet (a batch, or an expert's share of it).
+// meet as far as the call tells: a batch, or, by expert, the smaller of x's and
+// y's rows.  Sorted rows in order say T x E there where an expert has T at most,
+// and so take wider tiles than they fill: 16 tokens on 64 experts of 2048 x 256
+// 15.3 us, by perm 13.5.
 template <typename T, int G>
 cudaError_t q4_run(q4::Args& a, long long most, cudaStream_t st) {
   constexpr bool kF32 = sizeof(T) == 4;   // three pieces of x: two tiles of rows of x, one of W at most, by shared memory

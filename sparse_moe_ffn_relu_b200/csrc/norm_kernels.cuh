@@ -372,8 +372,10 @@ struct FwdArgs {
 };
 
 // Forward.  Measured: 4096 x 4096 bf16 with a full gate 27.6 us, 6.1 TB/s of the
-// 168 MB it has to move (94 % of a copy's rate); one token of 2048 columns
-// 2.5 us, which is the launch and four dependent latencies.
+// 168 MB it has to move (94 % of a copy's rate); 8192 x 2048 with a gate per
+// channel 24 us in bf16, 47 us in fp32 (86 and 88 %); one token of 2048 columns
+// 2.7 us, which is the launch and four dependent latencies.  VEC = 1 waits for
+// each row's own loads: 8192 x 2047 bf16 84 us, fp32 64 us.
 // pieces of 16 bytes a thread has in a slot of the ring
 template <typename T, bool FULL>
 constexpr int kFwdPieces = (FULL ? 3 : 2) * (int)sizeof(T) / 2;
@@ -493,8 +495,10 @@ struct BwdArgs {
 // dg_post = S gate, dgate = S g_post; otherwise S = sum_t c dx gate y r_y = dg_post.
 // Backward.  Measured: 8192 x 2048 bf16 with a gate per channel 48 us with
 // kn_reduce, of which 35 us grow with the rows (5.7 TB/s, 89 % of a copy's rate;
-// 32768 rows take 156 us) and 13 us do not: filling and draining the rings, the
-// partial sums' way through L2 and kn_reduce's latencies.
+// 32768 rows take 156 us) and 13 us do not.  Seen of those: kn_reduce, about 4 us,
+// and the partial sums, which leave as single floats 32 bytes apart; the rings'
+// filling and draining is the likely rest.  In fp32 68 us (91 % of a copy's rate).
+// VEC = 1 has no rows on their way: 8192 x 2047 bf16 146 us, fp32 83 us.
 template <typename T, typename TH, typename TR, bool FULL>
 constexpr int kBwdPieces = ((FULL ? 3 : 2) * (int)sizeof(T) + (int)sizeof(TH) + (int)sizeof(TR)) / 2;
 

@@ -12,15 +12,19 @@
 // group, so the only roundings are those of fp32 sums.  fp32 x enters as three
 // bf16 pieces whose sum is exact.
 //
-// Measured (codes from L2): one token, 2048 x 1024: 3.4 us, the launch and three
-// dependent latencies.  16 tokens, 17408 x 2048: 11 us, 1.8 TB/s of weights (28 %
-// of a copy's rate); 16 tokens on the 63 experts of 256 x 2048 that a router
-// activates 12 us.  8 tokens, 139264 x 2048: 42 us, 3.6 TB/s.  The bound there is
-// not DRAM but the integer pipe and issue slots: a step (32 rows x 128 codes a
-// warp) is 374 instructions for 8 tokens, 112 of them the shifts and logic
-// operations of unpacking (two cycles each on a quarter SM), 64 subtractions, 16
-// tensor operations.  Unpacking once for more rows of x, not wider loads, is what
-// would help; at 32 tokens a step serves four tiles of them.
+// Measured (codes from L2): one token, 2048 x 1024: 3.5 us, the launch and three
+// dependent latencies.  16 tokens, 17408 x 2048: 11 us, 1.7 TB/s of weights (26 %
+// of a copy's rate), and 16 tokens on the 63 experts of 256 x 2048 that a router
+// activates 12 us.  What bounds these is what surrounds the steps (32 rows x 128
+// codes a warp): a warp makes four in its life, and of the 678 warp instructions
+// that come to each about 250 unpack (112 shifts and logic operations, 64
+// subtractions), multiply (32 tensor operations, 8 loads of x) and scale; the
+// others make the table of units, stage x, form addresses and add the warps'
+// sums.  1 and 8 tokens, 139264 x 2048: 40 and 43 us, 3.5 TB/s (54 %), at 374
+// instructions a step: about 25 us of the busiest scheduler's issue slots and 22
+// of its integer pipe, neither full, as four warps a scheduler do not cover each
+// other's waits.  Every 8 NT rows of x (32 in bf16, 16 in fp32) read and unpack
+// all of W again: 64, 256 and 2048 rows of 17408 x 2048 take 29, 103 and 754 us.
 //
 // Layout: rows padded to Kp, a multiple of 128.  A block of 128 codes is 16
 // words of 8; word w sits at place 4 (w % 4) + w / 4, so that the 16 bytes
